@@ -1613,7 +1613,9 @@ __global__ void __launch_bounds__(NTHREADS, (target_ctas<MODE, D, NJ, NT, VAR>()
           float wmx = smx;
 #pragma unroll
           for (int o2 = 16; o2 > 0; o2 >>= 1) wmx = fmaxf(wmx, __shfl_xor_sync(0xffffffffu, wmx, o2));
-          const float nev = (wmx > 0.f) ? pow2i(max(-100, min(100, 13 - exp2_floor(wmx)))) : 1.f;
+          // (tokens without a scale, hidden ones or constant rows, leave the choice to
+          // the next step: their P' are zero under any normalizer)
+          const float nev = (wmx > 0.f) ? pow2i(max(-100, min(100, 13 - exp2_floor(wmx)))) : evs;
           const float fac = (evs == 0.f) ? 0.f : nev / evs;
           evs = nev;
           a_lo *= fac;
