@@ -325,7 +325,8 @@ bool valid_mod(const kvq_score_mod* m) {
 }
 
 void set_mod(AttendParams& p, const kvq_score_mod* m, long long pos0) {
-  // a cap so small that 2 / cap overflows, or so large that cap log2(e) does, keeps its limit's finite neighbour
+  // where cap log2(e) or 2 / cap would overflow, the largest finite number stands for it: the caps near 2^127 leave
+  // every logit as it is, those near 2^-127 make every logit 0, to fp32's rounding
   p.cap2 = m->softcap > 0.f ? std::fmin(m->softcap * 1.4426950408889634f, 3.4e38f) : 0.f;
   p.cap_f = m->softcap > 0.f ? std::fmin(2.0f / m->softcap, 3.4e38f) : 0.f;
   p.window = m->window;

@@ -114,12 +114,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // A capped score in base-2 logits: cap tanh(y / cap) with
 // x = y log2(e) is cap2 (1 - 2 / (2^(x f) + 1)), cap2 = cap log2(e) and
 // f = 2 / cap: two hardware approximations (2^x, 1/x), each within 2^-22, so
-// within cap2 2^-22 of the tanh; an overflowing 2^x gives +cap2.
+// within cap2 2^-22 of the tanh; an overflowing 2^x gives +cap2.  (The 2 stays
+// with the reciprocal, so that no finite cap2 overflows.)
 __device__ __forceinline__ float soft_cap(float x, float cap2, float f) {
   float r;
   const float e1 = fast_exp2(x * f) + 1.f;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e1));
-  return fmaf(-2.f * cap2, r, cap2);
+  return fmaf(-cap2, 2.f * r, cap2);
 }
 
 // Two fp32 at a time.
@@ -156,10 +157,17 @@ __device__ __forceinline__ float2 cap_poly(float2 x, float2 inv) {
 }
 constexpr float kCapPoly = 0.70710678f;   // up to this share of the cap
 __device__ __forceinline__ float cap_inverse(float f) { return 0.5f * f * 0.69314718055994531f; }   // 1 / cap2
-__device__ __forceinline__ float any_cap(float x, float cap2, float f) {
-  const float inv = cap_inverse(f), near = cap_poly(make_float2(x, x), make_float2(inv, inv)).x;
-  return fabsf(x) > kCapPoly * cap2 ? soft_cap(x, cap2, f) : near;
+// Each value by the form that suits its size: off by 2^-20 of the result at any cap.
+__device__ __forceinline__ float2 any_cap2(float2 x, float cap2, float f) {
+  const float inv = cap_inverse(f);
+  const float2 near = cap_poly(x, make_float2(inv, inv));
+  return make_float2(fabsf(x.x) > kCapPoly * cap2 ? soft_cap(x.x, cap2, f) : near.x,
+                     fabsf(x.y) > kCapPoly * cap2 ? soft_cap(x.y, cap2, f) : near.y);
 }
+__device__ __forceinline__ float any_cap(float x, float cap2, float f) { return any_cap2(make_float2(x, x), cap2, f).x; }
+// Up to this cap (64, times log2 e) the first form alone is within 2.2e-5 of a
+// logit, whatever the logit's size.
+constexpr float kCapShort = 64.f * 1.4426950408889634f;
 
 // ------------------------------------------------------------------------------
 // Thread-block clusters: the hardware cluster barrier (every thread of every
