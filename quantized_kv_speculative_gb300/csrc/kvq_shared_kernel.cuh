@@ -819,13 +819,15 @@ __global__ void __launch_bounds__(Shape<NR>::THREADS, Shape<NR>::CTAS) shared_ke
         }
         if constexpr (MOD) {
           if (p.cap2 > 0.f) {
+            // The polynomial alone where no row comes near the cap; else each logit by
+            // the form that suits its size, so that none is touched by its neighbours'.
+            // (Lanes past the last token hold minus infinity and ask for nothing.)
             float big = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
-            if (__any_sync(0xffffffffu, big > kCapPoly * p.cap2)) {   // (infinite past the last token)
+            if (__any_sync(0xffffffffu, valid && big > kCapPoly * p.cap2)) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[k] = make_float2(soft_cap(x[k].x, p.cap2, p.cap_f), soft_cap(x[k].y, p.cap2, p.cap_f));
+              for (int k = 0; k < 4; ++k) x[k] = any_cap2(x[k], p.cap2, p.cap_f);
             } else {
               const float inv = cap_inverse(p.cap_f);
 #pragma unroll

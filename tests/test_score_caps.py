@@ -1,9 +1,11 @@
-"""Caps from tight to far above the logits, over quantized, residual and pending tokens.
+"""Caps from tight to far above the logits, over quantized, residual and pending tokens and over a shared prefix.
 
 Tolerance: a capped logit is off by what the cap's argument is off and by 2^-20 of its own size, whatever the cap (below 0.7 of the
 cap a polynomial within 4.6e-7 of the value; above, two approximations within 2^-22 of the cap each).  |logit| is at most
 ``size`` = scale sum |q| |k|, so ``extra`` = 2^-20 of that stands in the place of the 2^-20 cap that the comparison allows elsewhere."""
+import numpy as np
 import pytest
+import torch
 
 import kvq_inputs as ki
 import quantized_kv_speculative_gb300 as kvq
@@ -12,6 +14,7 @@ from quantized_kv_speculative_gb300 import _build
 from plain_attention import assert_close, attend_plain, build
 
 EXTRA = 2.0 ** -20
+EXTRA_V = 2.0 ** -9   # the shared pass's values and weights, in fp16 each
 
 
 @pytest.fixture(scope="module")
@@ -62,3 +65,59 @@ def test_caps_below_every_logit(lib, cap):
     gc, ocs = build("hier8", [300], 2, 64, 32, seed=3)
     q = ki.queries(3, 1, 1, 4, 64)
     assert_close(*kvq.kvq_attend_mod(gc, "int8", dev(q), kvq.ScoreMod(cap)), attend_plain(ocs, "int8", 0 * q))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [1e-45, 1e-38, 1e-30])
+def test_caps_below_every_logit_over_a_prefix(lib, cap):
+    pc, (po,) = build("hier8", [200], 2, 64, 32, seed=4, ragged=False)
+    gc, ocs = build("hier8", [300], 2, 64, 32, seed=3)
+    q = ki.queries(3, 1, 1, 4, 64)
+    out, lse = kvq.kvq_attend_shared(pc, gc, "int8", dev(q), mod=kvq.ScoreMod(cap))
+    assert_close(out, lse, attend_plain(ocs, "int8", 0 * q, prefix=po), extra_v=EXTRA_V)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("mode,n0,B,hg", [("int8", 37, 2, 2), ("int4", 300, 3, 1), ("int2", 1000, 11, 4), ("int8", 700, 20, 4)])
+def test_loose_caps_over_a_prefix(lib, mode, n0, B, hg, cap):
+    """Prefixes that end inside a tile, whose last lanes hold no token."""
+    fmt = kvq.MODE_FORMAT[mode]
+    pc, (po,) = build(fmt, [n0], 1, 64, 32, seed=5, ragged=False)
+    gc, ocs = build(fmt, [40 + i for i in range(B)], 1, 64, 32, seed=6)
+    q = ki.queries(5, B, 1, hg, 64)
+    out, lse = kvq.kvq_attend_shared(pc, gc, mode, dev(q), mod=kvq.ScoreMod(cap))
+    assert_close(out, lse, bounded((ocs, mode, q), dict(prefix=po), cap), extra=EXTRA, extra_v=EXTRA_V)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [1e3, 1e6, 1e30])
+def test_a_row_past_the_cap_leaves_the_others_alone(lib, cap):
+    """A padded row of the largest values, or one at the cap, beside ordinary rows: the others' log-sum-exps stay within their own
+    logits' bound, not the cap's."""
+    pc, (po,) = build("hier8", [600], 1, 64, 32, seed=7, ragged=False)
+    gc, ocs = build("hier8", [40] * 4, 1, 64, 32, seed=8, ragged=False)
+    q = ki.queries(7, 4, 1, 2, 64)
+    for odd in (3e38, float(min(cap, 1e37))):
+        qd = dev(q)
+        qd[1] = odd
+        qd[2] = -odd
+        out, lse = kvq.kvq_attend_shared(pc, gc, "int8", qd, mod=kvq.ScoreMod(cap))
+        good = [0, 3]
+        assert_close(out[good], lse[good], bounded(([ocs[b] for b in good], "int8", q[good]), dict(prefix=po), cap), extra=EXTRA, extra_v=EXTRA_V)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [20.0, 64.0])
+def test_ordinary_caps_over_a_prefix_that_ends_inside_a_tile(lib, cap):
+    """One key seen: its capped logit is the log-sum-exp, off by 2^-20 of itself also where lanes of the tile hold no token."""
+    pc, (po,) = build("hier8", [37], 2, 64, 32, seed=9, ragged=False)
+    gc, ocs = build("hier8", [0, 0], 2, 64, 32, seed=9, ragged=False)
+    q = ki.queries(9, 2, 1, 4, 64) * np.float32(0.05)
+    q = ki.round_bf16(q)
+    first = torch.tensor([36, 36], dtype=torch.int32, device="cuda")
+    out, lse = kvq.kvq_attend_shared(pc, gc, "int8", dev(q), mod=kvq.ScoreMod(cap, first=first))
+    want, want_lse, delta, vmax = bounded((ocs, "int8", q), dict(prefix=po, first=[36, 36]), cap)
+    off = np.abs(lse.cpu().numpy().astype(np.float64) - want_lse)
+    assert np.all(off <= delta + (2.0 ** -20 + 2.0 ** -22) * np.abs(want_lse) + 2.0 ** -24 * 4), off.max()
+    assert_close(out, None, (want, want_lse, delta, vmax), extra=EXTRA, extra_v=EXTRA_V)
