@@ -90,7 +90,9 @@ __device__ __forceinline__ void store_words(uint16_t* p, const uint32_t* w) {
 
 template <int VW, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 table[kRopeTokens * kMaxPairs];   // (m cos, m sin) of token x pair
+  // (m cos, m sin) of token x pair, read two pairs at a time
+  __shared__ __align__(sizeof(float4)) float2 table[kRopeTokens * kMaxPairs];
+  static_assert(__alignof__(table) >= sizeof(float4) && kMaxPairs % 2 == 0, "a token's pairs start at a vector of four floats");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
