@@ -565,9 +565,9 @@ kvq_status kvq_rope_init(kvq_rope* rope, const kvq_rope_desc* desc, const double
  * its own input where both have the same layout; otherwise outputs overlap
  * neither inputs nor one another.  n_tokens = 0 does nothing.  Enqueues one
  * kernel.  Errors, before any launch: KVQ_ERR_NOT_INITIALIZED;
- * KVQ_ERR_INVALID_ARG for null or misaligned pointers (16 bytes), strides that
- * are negative, above 2^40 or not multiples of 8, bad counts, B n_tokens >=
- * 2^31, or an overlap.
+ * KVQ_ERR_INVALID_ARG for null or misaligned pointers (16 bytes), strides (of
+ * dimensions longer than one) that are negative, above 2^40 or not multiples of
+ * 8, bad counts, B n_tokens >= 2^31, or an overlap.
  */
 kvq_status kvq_rope_apply(const kvq_rope* rope, const void* q, const int64_t* q_strides, int32_t num_q_heads,
                           void* q_out, const void* k, const int64_t* k_strides, int32_t num_kv_heads, void* k_out,

@@ -284,15 +284,19 @@ kvq_status kvq_rope_apply(const kvq_rope* rope, const void* q, const int64_t* q_
     if (n_tokens == 0) continue;
     if (!in[w] || !out[w] || !strides[w] || (reinterpret_cast<uintptr_t>(in[w]) & 15u) || (reinterpret_cast<uintptr_t>(out[w]) & 15u))
       return KVQ_ERR_INVALID_ARG;
-    for (int a = 0; a < 3; ++a)
-      if (strides[w][a] < 0 || strides[w][a] % 8 || strides[w][a] > kMaxStride) return KVQ_ERR_INVALID_ARG;
-    const double ext = extent_bytes(strides[w], batch, n_tokens, heads[w], D);
+    int64_t st[3];   // nothing steps along a dimension of one entry, whatever its stride
+    const int size[3] = {batch, n_tokens, heads[w]};
+    for (int a = 0; a < 3; ++a) {
+      st[a] = size[a] > 1 ? strides[w][a] : 0;
+      if (st[a] < 0 || st[a] % 8 || st[a] > kMaxStride) return KVQ_ERR_INVALID_ARG;
+    }
+    const double ext = extent_bytes(st, batch, n_tokens, heads[w], D);
     if (ext > kMaxExtent) return KVQ_ERR_INVALID_ARG;
     p.in[w] = static_cast<const uint16_t*>(in[w]);
     p.out[w] = static_cast<uint16_t*>(out[w]);
-    p.sb[w] = strides[w][0];
-    p.st[w] = strides[w][1];
-    p.sh[w] = strides[w][2];
+    p.sb[w] = st[0];
+    p.st[w] = st[1];
+    p.sh[w] = st[2];
     rin[w] = {reinterpret_cast<uintptr_t>(in[w]),
               reinterpret_cast<uintptr_t>(in[w]) + static_cast<uintptr_t>(ext)};
     rout[w] = {reinterpret_cast<uintptr_t>(out[w]),
