@@ -546,7 +546,7 @@ typedef struct kvq_rope {
  * way).  Host arithmetic in 64 bits; the position's whole turns drop out
  * exactly, so far positions lose no precision.  Errors: KVQ_ERR_INVALID_ARG
  * for a null struct or descriptor, a field outside the ranges above, or a
- * frequency that is not finite. */
+ * frequency that is not finite, before or after its scaling. */
 kvq_status kvq_rope_init(kvq_rope* rope, const kvq_rope_desc* desc, const double* inv_freq);
 
 /*

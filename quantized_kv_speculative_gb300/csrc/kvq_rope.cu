@@ -248,6 +248,7 @@ kvq_status kvq_rope_init(kvq_rope* rope, const kvq_rope_desc* d, const double* i
       w = std::fmin(1.0, std::fmax(0.0, (d->original_len * std::fabs(f[i]) / kTwoPi - d->low) / (d->high - d->low)));
     }
     if (w < 1.0) f[i] = f[i] * w + f[i] / d->factor * (1.0 - w);
+    if (!std::isfinite(f[i])) return KVQ_ERR_INVALID_ARG;   // a factor near 0
   }
   std::memset(rope, 0, sizeof(*rope));
   rope->desc = *d;
