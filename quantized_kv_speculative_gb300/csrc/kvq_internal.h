@@ -106,6 +106,11 @@ struct AttendParams {
 // The pass of every sequence's rows over the shared prefix (kvq_attend_shared).
 constexpr int kSharedTile = 128;        // prefix tokens per tile
 constexpr int kMaxSharedSplits = 64;    // splits of the prefix's tiles per KV head
+// A split's weighted values are summed in one chain of the tensor cores' fp32
+// accumulators, which cut each of its steps (16 tokens) off towards zero, by
+// 2^-23 of the sum at most: a bias that grows with the chain.  So a split has 64
+// tiles at most (512 steps, 2^-14 of the sum), as long as kMaxSharedSplits allow.
+constexpr int kSharedChainTiles = 64;
 struct SharedParams {
   CacheView c;              // the prefix: batch 1, not ragged
   CacheView own;            // the sequences' own caches: lengths (query positions) alone are read
@@ -134,7 +139,7 @@ struct SharedPlan {
   int row_tiles, cols;      // CTAs over the rows, and padded rows of each
 };
 SharedPlan shared_plan(const kvq_cache_desc& prefix, int rows, int tiles);
-// The most splits that shared_plan gives for any number of tiles.
+// The most splits that shared_plan gives at any fill of the prefix.
 int shared_splits_max(const kvq_cache_desc& prefix, int rows);
 // Floats of the zero terms of one key group (all row tiles).
 int shared_zero_floats(int rows);

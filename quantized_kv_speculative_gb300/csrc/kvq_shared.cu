@@ -22,15 +22,23 @@ void shared_rows(int rows, SharedPlan* pl) {
   pl->cols = per <= 16 ? 16 : ceil_div_i(per, 32) * 32;
 }
 
+// The most splits for a number of tiles: one CTA fits an SM (two with up to 32
+// rows), and the splits fill the SMs once, or as many times as keep each split's
+// chain of sums short (whole waves, so that the last one is as full as the first).
+int most_splits(int heads, const SharedPlan& pl, long long tiles) {
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  const long long units = static_cast<long long>(heads) * pl.row_tiles;
+  const int wave = static_cast<int>(std::max(1LL, std::min<long long>(kMaxSharedSplits, sms * (pl.cols <= 32 ? 2 : 1) / units)));
+  return wave * std::min(kMaxSharedSplits / wave, std::max(1, ceil_div_i(tiles, static_cast<long long>(kSharedChainTiles) * wave)));
+}
+
 }  // namespace
 
-// One CTA fits an SM (two with up to 32 rows), and the splits fill the SMs once.
 int shared_splits_max(const kvq_cache_desc& prefix, int rows) {
   SharedPlan pl{};
   shared_rows(rows, &pl);
-  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
-  const long long units = static_cast<long long>(prefix.num_kv_heads) * pl.row_tiles;
-  return static_cast<int>(std::max(1LL, std::min<long long>(kMaxSharedSplits, sms * (pl.cols <= 32 ? 2 : 1) / units)));
+  // the most tiles: all of the capacity, and the residual's up to 2 G - 1 tokens
+  return most_splits(prefix.num_kv_heads, pl, ceil_div_i(prefix.capacity_tokens, kSharedTile) + ceil_div_i(2 * prefix.group_size - 1, kSharedTile));
 }
 
 int shared_zero_floats(int rows) {
@@ -42,8 +50,7 @@ int shared_zero_floats(int rows) {
 SharedPlan shared_plan(const kvq_cache_desc& prefix, int rows, int tiles) {
   SharedPlan pl{};
   shared_rows(rows, &pl);
-  const int most = shared_splits_max(prefix, rows);
-  pl.per = std::max(1, ceil_div_i(tiles, most));
+  pl.per = std::max(1, ceil_div_i(tiles, most_splits(prefix.num_kv_heads, pl, tiles)));
   pl.S = ceil_div_i(tiles, pl.per);
   return pl;
 }

@@ -38,8 +38,15 @@
 // multiply-add, both multiplied with Q.  The part q.(z + c0 s) is one number
 // per row and key group: a small launch ahead (zero_kernel) leaves them in the
 // workspace, and each tile's arrive with its codes.  Q is bf16, exact in f16
-// after a power of two of the row's own.  Values and weights are one f16 each (2^-11): the
-// output is bf16.
+// after a power of two of the row's own.  Values and weights are one f16 each: off by
+// 2^-12 to 2^-11 of themselves at random, where the splits of kvq_attend keep codes
+// exact and weights in two parts.  Against 64 bits that makes the output 1% less
+// exact (1.66e-3 -> 1.68e-3 of its size at 32K, nearly all of it bf16's rounding);
+// second parts would double the products and the stores into TMEM.  Weighted values
+// are summed in TMEM over a split, in steps of 16 tokens that are cut off towards
+// zero: at most 2^-23 of the sum each, 2e-5 of |v| measured over 512 steps, 7e-5 over
+// 8,192 and 1.4e-4 over 16,384 (sums that climb and fall back).  The plan keeps a
+// split at 512 steps as long as 64 splits allow (270,000 tokens at least).
 //
 // Softmax.  Row maxima run across lanes here, so they are looked at only when
 // needed: a row keeps a reference m and its weights are 2^(x - m), m set 4 below
