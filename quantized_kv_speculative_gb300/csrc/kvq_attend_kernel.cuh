@@ -300,7 +300,7 @@ __device__ void prefix_partial(const AttendParams& p, int b, int kvh, int lo, in
 #pragma unroll
     for (int o2 = 16; o2 > 0; o2 >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o2);
     if (lane == 0) {
-      dst[rho] = M;
+      dst[rho] = L == L ? M : L;   // (a row that is no number has no maximum either)
       dst[kMaxRows + rho] = L;
     }
   }
@@ -343,7 +343,7 @@ __device__ void prefix_partial(const AttendParams& p, int b, int kvh, int lo, in
 template <int D>
 __device__ __forceinline__ void join_prefix(const float* pre, int rho, int d4, float4& acc, float& M, float& L) {
   const float m = pre[rho], top = fmaxf(M, m);
-  if (top == neg_inf()) return;
+  if (M == neg_inf() && m == neg_inf()) return;
   const float own = (M == neg_inf()) ? 0.f : L * fast_exp2(M - top), f = (m == neg_inf()) ? 0.f : fast_exp2(m - top);
   const float4 x = *reinterpret_cast<const float4*>(pre + 2 * kMaxRows + rho * D + 4 * d4);
   const float sum = fmaf(f, pre[kMaxRows + rho], own), inv = (sum > 0.f) ? 1.f / sum : 0.f;

@@ -1019,7 +1019,8 @@ __global__ void __launch_bounds__(Shape<NR>::THREADS, Shape<NR>::CTAS) shared_ke
       const int mine = min(cw, nrow - c0);     // rows of this group (may be negative)
       if (ln < mine) {
         const float sum = (wm[ln] + wm[NR + ln]) + (wm[2 * NR + ln] + wm[3 * NR + ln]);
-        reinterpret_cast<float2*>(p.ml)[part + ln] = make_float2(sum > 0.f ? -nref[ln] : neg_inf(), sum);
+        // (a sum that is no number keeps its reference, and so its place among the partials)
+        reinterpret_cast<float2*>(p.ml)[part + ln] = make_float2(sum == 0.f ? neg_inf() : -nref[ln], sum);
       }
       if (nt > 0) {
         const float f = pow2f_exact(value_exp());
