@@ -366,9 +366,44 @@ class ScoreMod:
 
     def __init__(self, softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
                  first: Optional[torch.Tensor] = None):
-        self.slopes, self.first = slopes, first   # kept alive with the struct that points at them
-        self.struct = KvqScoreMod(softcap, window, _ptr(slopes, torch.float32, "slopes"),
-                                  _ptr(first, torch.int32, "first"), 0)
+        self.struct = KvqScoreMod()
+        self.softcap, self.window, self.slopes, self.first = softcap, window, slopes, first
+
+    # What is set later counts for the calls after it: the struct follows, and
+    # the tensors stay alive with the struct that points at them.
+    @property
+    def softcap(self) -> float:
+        return float(self.struct.softcap)
+
+    @softcap.setter
+    def softcap(self, value: float):
+        self.struct.softcap = value
+
+    @property
+    def window(self) -> int:
+        return int(self.struct.window)
+
+    @window.setter
+    def window(self, value: int):
+        self.struct.window = value
+
+    @property
+    def slopes(self) -> Optional[torch.Tensor]:
+        return self._slopes
+
+    @slopes.setter
+    def slopes(self, value: Optional[torch.Tensor]):
+        self.struct.slopes = _ptr(value, torch.float32, "slopes")
+        self._slopes = value
+
+    @property
+    def first(self) -> Optional[torch.Tensor]:
+        return self._first
+
+    @first.setter
+    def first(self, value: Optional[torch.Tensor]):
+        self.struct.first = _ptr(value, torch.int32, "first")
+        self._first = value
 
     def check(self, num_q_heads: int, batch: int):
         if self.slopes is not None and self.slopes.shape != (num_q_heads,):
