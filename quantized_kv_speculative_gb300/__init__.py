@@ -385,7 +385,9 @@ class ScoreMod:
 
     @window.setter
     def window(self, value: int):
-        self.struct.window = value
+        if int(value) != ctypes.c_int32(int(value)).value:   # ctypes would keep its low bits
+            raise ValueError(f"a window of {value} is not an int32")
+        self.struct.window = int(value)
 
     @property
     def slopes(self) -> Optional[torch.Tensor]:

@@ -24,6 +24,16 @@ def test_numbers_follow():
     assert mod.slopes is None and mod.first is None and not mod.struct.slopes and not mod.struct.first
 
 
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32 + 5, 2 ** 40, -2 ** 31 - 1])
+def test_windows_past_32_bits_are_refused(window):
+    with pytest.raises(ValueError):
+        kvq.ScoreMod(window=window)
+    mod = kvq.ScoreMod(window=3)
+    with pytest.raises(ValueError):
+        mod.window = window
+    assert mod.window == 3 and kvq.ScoreMod(window=2 ** 31 - 1).window == 2 ** 31 - 1
+
+
 def test_a_refused_tensor_changes_nothing():
     mod = kvq.ScoreMod(30.0)
     for name in ("slopes", "first"):
