@@ -329,7 +329,8 @@ void set_mod(AttendParams& p, const kvq_score_mod* m, long long pos0) {
   // every logit as it is, those near 2^-127 make every logit 0, to fp32's rounding
   p.cap2 = m->softcap > 0.f ? std::fmin(m->softcap * 1.4426950408889634f, 3.4e38f) : 0.f;
   p.cap_f = m->softcap > 0.f ? std::fmin(2.0f / m->softcap, 3.4e38f) : 0.f;
-  p.window = m->window;
+  // a query may stand up to kMaxRows before position 0; a window's lower edge stays in 32 bits all the same
+  p.window = std::min(m->window, INT_MAX - kMaxRows);
   p.slopes = m->slopes;
   p.first = m->first;
   p.pos0 = pos0;

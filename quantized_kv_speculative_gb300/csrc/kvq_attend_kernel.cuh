@@ -160,8 +160,7 @@ __device__ __forceinline__ long long mod_qpos(const AttendParams& p, int b, int 
 }
 __device__ __forceinline__ int mod_low(const AttendParams& p, int b, int rho) {
   int lo = p.first ? p.first[b] : INT_MIN;
-  // (a query may stand before position 0, so that its window begins past 32 bits)
-  if (p.window > 0) lo = max(lo, static_cast<int>(max(static_cast<long long>(INT_MIN), mod_qpos(p, b, rho) - (p.window - 1))));
+  if (p.window > 0) lo = max(lo, static_cast<int>(mod_qpos(p, b, rho) - (p.window - 1)));
   return lo;
 }
 // A row's slope in base-2 logits (0 without slopes).

@@ -383,8 +383,7 @@ __global__ void __launch_bounds__(Shape<NR>::THREADS, Shape<NR>::CTAS) shared_ke
       const int row = row0 + e, b = row / p.R, rho = row % p.R;
       qp = n0 + static_cast<int>(seq_lq(p.own, b)) + seq_r(p.own, b) + p.P - p.gamma + rho / p.HG;
       lo = p.first ? p.first[b] : INT_MIN;
-      // (a query may stand before position 0, so that its window begins past 32 bits)
-      if (p.window > 0) lo = max(lo, static_cast<int>(max(static_cast<long long>(INT_MIN), static_cast<long long>(qp) - (p.window - 1))));
+      if (p.window > 0) lo = max(lo, qp - (p.window - 1));
       if (p.slopes) slope = p.slopes[kvh * p.HG + rho % p.HG] * 1.4426950408889634f;
       atomicMin(lo_all_s, lo);
       atomicMax(lo_any_s, lo);
