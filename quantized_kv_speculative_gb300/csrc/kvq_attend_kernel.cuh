@@ -1516,28 +1516,18 @@ __global__ void __launch_bounds__(NTHREADS, (target_ctas<MODE, D, NJ, NT, VAR>()
         }
         if constexpr (VAR == kVarMod) {
           if (p.cap2 > 0.f) {
-            // Caps up to 64 by the short form alone: off by 2.2e-5 at most, a weight by
-            // 1.5e-5 of itself, which the output's 2^-9 swallows.  Above, where 2^-22 of
-            // the cap would not be small, each logit by the form that suits its size (one
-            // INT4 token at 32K: 39.4 us, and 38.8 by the short form).
-            if (p.cap2 <= kCapShort) {
+            // Each logit by the form that suits its size, at any cap.  (The form for
+            // large ones alone, off by 2^-22 of the cap, would take 38.7 us, not 39.4, for
+            // one INT4 token at 32K; the choice by a vote of the warp 39.2, but 1% more in
+            // calls without a cap.)
 #pragma unroll
-              for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  x[s][nt][0] = soft_cap(x[s][nt][0], p.cap2, p.cap_f);
-                  x[s][nt][1] = soft_cap(x[s][nt][1], p.cap2, p.cap_f);
-                }
-            } else {
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const float2 c = any_cap2(make_float2(x[s][nt][0], x[s][nt][1]), p.cap2, p.cap_f);
-                  x[s][nt][0] = c.x;
-                  x[s][nt][1] = c.y;
-                }
-            }
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 c = any_cap2(make_float2(x[s][nt][0], x[s][nt][1]), p.cap2, p.cap_f);
+                x[s][nt][0] = c.x;
+                x[s][nt][1] = c.y;
+              }
           }
           if (p.slopes) {
 #pragma unroll

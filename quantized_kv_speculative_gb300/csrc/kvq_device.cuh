@@ -165,9 +165,6 @@ __device__ __forceinline__ float2 any_cap2(float2 x, float cap2, float f) {
                      fabsf(x.y) > kCapPoly * cap2 ? soft_cap(x.y, cap2, f) : near.y);
 }
 __device__ __forceinline__ float any_cap(float x, float cap2, float f) { return any_cap2(make_float2(x, x), cap2, f).x; }
-// Up to this cap (64, times log2 e) the first form alone is within 2.2e-5 of a
-// logit, whatever the logit's size.
-constexpr float kCapShort = 64.f * 1.4426950408889634f;
 
 // ------------------------------------------------------------------------------
 // Thread-block clusters: the hardware cluster barrier (every thread of every
