@@ -297,6 +297,10 @@ kvq_status kvq_attend(const kvq_cache* cache, kvq_mode mode, const void* q, int3
  * pending tokens, the causal rule of kvq_attend).  A cache's token t is at
  * position t, residual token i at Lq + i, pending token p at Lq + r + p, and
  * query i at Lq + r + n_pend - gamma + i, with the sequence's own lengths.
+ * The cap is exact to 2^-20 of a capped logit, whatever its size.
+ * kvq_topk and kvq_attend_topk know nothing of it: they rank by the plain
+ * scores, and may select tokens that a window or a first position hides (which
+ * kvq_attend_mod then hides, selected or not).
  */
 typedef struct kvq_score_mod {
   float softcap;         /* 0: no cap; else > 0, finite                          */
@@ -344,6 +348,12 @@ kvq_status kvq_attend_mod(const kvq_cache* cache, kvq_mode mode, const kvq_score
  *  KVQ_ERR_UNSUPPORTED for more heads than above or a batch above 262,144.
  *  A query that is not finite spoils its own rows only.  Enqueues at most three
  *  kernels.
+ *  Precision: the prefix's keys are held to 22 bits, but its values c s + z (off
+ *  by 2^-11 of |c s|, of |z| and of themselves at most) and their weights (2^-11)
+ *  in one fp16 each, where kvq_attend keeps codes exact and weights in two parts;
+ *  the output's error against 64 bits, nearly all of it bf16's rounding, grows by
+ *  about 1%.  Values are held relative to the largest |v| that any query of the
+ *  batch sees in a split of the prefix; one 2^27 below it begins to lose bits.
  */
 kvq_status kvq_attend_shared(const kvq_cache* prefix, const kvq_cache* cache, kvq_mode mode, const kvq_score_mod* mod,
                              const void* q, int32_t num_q_heads, int32_t gamma, const void* pend_k, const void* pend_v,

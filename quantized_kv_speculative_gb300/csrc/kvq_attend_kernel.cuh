@@ -56,12 +56,15 @@
 // sequence's first visible one on (rounded down to a split boundary), so a
 // window's bytes are all that is read.
 // Measured on the GB300 in a graph (kvq_attend without the changes in brackets):
-// INT4, one token at 32K, 32 heads, capped 38.1 us (33.5: the cap's two special
-// functions a logit, and codes as normal numbers); INT8, 8 tokens at 8K, biased
-// 26.4 (23.2); INT8, 6 tokens, a window of 4,096 at 128K 18.9 (204 for the whole);
-// INT2, 36 sequences up to 32K seen from a first position on 288 (495 for the whole).
-// Bound as the plain variant is: by instructions at 32K and for the batch, by the
-// launch's fixed 10 us or so (first loads, combine) for short ranges.
+// INT4, one token at 32K, 32 heads, capped 39.4 us (33.5: the cap's polynomial and
+// special functions, and codes as normal numbers); INT8, 8 tokens at 8K, biased
+// 26.6 (23.2); INT8, 6 tokens, a window of 4,096 at 128K, capped 19.6 (204 for the
+// whole); INT2, 36 sequences up to 32K seen from a first position on 241 (496 for
+// the whole).  Neither the issue slots (1.8 to 2.1 of 4 used) nor HBM (0.2 to 0.6)
+// are full: what is left is latency within a warp's chain of products, softmax and
+// products, and, for short ranges, the launch's fixed 10 us or so and a kernel
+// whose code is fetched cold for one or two tiles a warp (warps wait for
+// instructions 2 to 6 cycles an issue).
 #include <limits.h>
 
 #include "kvq_modes.cuh"

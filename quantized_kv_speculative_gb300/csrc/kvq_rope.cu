@@ -8,8 +8,9 @@
 // Angles are kept in turns as 64-bit fixed-point fractions: with
 // T_i = frac(f_i / 2 pi) 2^64, the low 64 bits of p T_i are the fraction of a
 // turn at position p, whatever whole turns were made, in one integer product.
-// The upper 32 bits become a signed fp32 fraction of a turn, so the angle is
-// exact to 2^-24 of its value in (-pi, pi] at every position (an fp32 product
+// The upper 32 bits become a signed fp32 fraction of a turn, so the angle in
+// (-pi, pi] is off by 2^-32 of a turn and 2^-24 of itself at every position, and
+// by what T_i's 53 bits leave, 2^-53 of a turn a position at most (an fp32 product
 // p f_i would be off by 0.03 radians at position 500,000).
 //
 // Bound by memory: each query and key value is read and written once.  The

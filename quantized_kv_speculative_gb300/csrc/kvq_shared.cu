@@ -22,9 +22,10 @@ void shared_rows(int rows, SharedPlan* pl) {
   pl->cols = per <= 16 ? 16 : ceil_div_i(per, 32) * 32;
 }
 
-// The most splits for a number of tiles: one CTA fits an SM (two with up to 32
-// rows), and the splits fill the SMs once, or as many times as keep each split's
-// chain of sums short (whole waves, so that the last one is as full as the first).
+// The most splits for a number of tiles.  A unit is a KV head's row tile.  One CTA
+// fits an SM (two with up to 32 rows); a wave has as many splits of each unit as fit
+// the SMs together, rounded down (96 units leave 56 of 152 SMs without work), and
+// there are as many whole waves as keep each split's chain of sums short.
 int most_splits(int heads, const SharedPlan& pl, long long tiles) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const long long units = static_cast<long long>(heads) * pl.row_tiles;

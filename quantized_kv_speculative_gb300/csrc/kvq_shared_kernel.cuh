@@ -23,9 +23,11 @@
 // values turned in one phase, or two halves of the warps in opposite phases,
 // took 5 to 20% longer.
 //
-// Bound by instructions: of the 4,500 cycles of a tile at 96 rows (INT2, G = 32)
-// some 1,250 each go to keys, values and the softmax, at 2.4 instructions a cycle
-// of an SM; the tensor cores are busy for a fifth.  Measured on the GB300 in a
+// Bound by the phases' latency: of the 4,500 cycles of a tile at 96 rows (INT2,
+// G = 32) some 1,250 each go to keys, values and the softmax, one after another, at
+// 2.4 instructions a cycle of an SM (of 4); the tensor cores are busy for a fifth,
+// HBM for less.  Fewer instructions alone no longer help (35 of 800 a warp and tile:
+// nothing); phases that overlap would.  Measured on the GB300 in a
 // graph (both launches): 16 rows x 32 heads over 8K INT4 tokens 32 us; 288 rows x
 // 8 heads over 32K INT2 tokens 102 us (0.38 PFLOP/s of the two products, 0.57 with
 // the keys' second part; in tiles of 96 rows, each of which turns the codes again,
@@ -1064,13 +1066,14 @@ __global__ void __launch_bounds__(Shape<NR>::THREADS, Shape<NR>::CTAS) shared_ke
 // k order is permuted so that a lane's operands are 8 adjacent channels: k-step
 // 2 j + i, register halves e of lane q hold channels 32 j + 8 q + 4 i + 2 e.
 // Bound by its loads' latency: 3 to 12 us, most of them beside the start of the
-// pass.  (288 rows over 1,025 groups x 8 heads, whole call: CTAs of 64 rows
-// 143.9 us, of 32 rows 146.4; a loop over all row tiles 143.2 to 148 by its grid.)
+// pass.  (288 rows over 1,025 groups x 8 heads, whole call, when it took three row
+// tiles of 96, which two of 160 have replaced (134 us): CTAs of 64 rows 143.9 us, of
+// 32 rows 146.4; a loop over all row tiles 143.2 to 148 by its grid.)
 // ------------------------------------------------------------------------------
 template <int D, int NR>
 __global__ void __launch_bounds__(128) zero_kernel(const __grid_constant__ SharedParams p, float add) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int qoff[NR];   // element offset of each row's query, -1: none
+  __shared__ int qoff[NR];   // each row's place among the queries (in rows of D), -1: none
   const int lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
   constexpr int PARTS = (NR + 63) / 64;   // CTAs over a tile's rows
   const int rt = blockIdx.y / PARTS, m0 = blockIdx.y % PARTS * 64, kvh = blockIdx.z, G = p.c.G;
